@@ -26,6 +26,7 @@
 namespace {
 
 PyObject* g_error = nullptr;  // NF4KVError(code, where)
+PyObject* g_parts[5];         // the names of an NF4KVCache's parts
 
 struct Refused : std::runtime_error {
     using std::runtime_error::runtime_error;
@@ -78,20 +79,71 @@ void* stream_for(std::initializer_list<PyObject*> given) {
     return stream.stream();
 }
 
-// What an NF4KVCache hands over.
+uint16_t* bf16(const at::Tensor& t) { return static_cast<uint16_t*>(t.data_ptr()); }
+
+// An NF4KVCache as it stands at the call: its tensors are ordinary attributes,
+// copied, moved, replaced and resized like any others, so that their addresses
+// hold for one call only.  (Read and checked anew: 0.2 us.)
 struct Held {
     nf4_kv_cache c;
     int64_t device;  // -1: no GPU
+
+    explicit Held(PyObject* cache) {
+        for (int i = 0; i < 5; ++i) {
+            own[i] = PyObject_GetAttr(cache, g_parts[i]);
+            if (!own[i]) {
+                drop();
+                if (!PyErr_ExceptionMatches(PyExc_AttributeError)) throw PythonError{};
+                PyErr_Clear();
+                throw Refused("cache: an NF4KVCache");
+            }
+        }
+        try {
+            fill();
+        } catch (...) {
+            drop();
+            throw;
+        }
+    }
+    ~Held() { drop(); }
+    Held(const Held&) = delete;
+    Held& operator=(const Held&) = delete;
+
+   private:
+    PyObject* own[5] = {};
+
+    void drop() {
+        for (PyObject* o : own) Py_XDECREF(o);
+    }
+
+    void fill() {
+        const char* const codes = "codes: contiguous uint8 [pages, heads, page, dim/2]";
+        const char* const scales = "scales: contiguous bf16 [pages, heads, page, dim/64]";
+        const at::Tensor &kc = tensor(own[0], codes), &ks = tensor(own[1], scales), &vc = tensor(own[2], codes),
+                         &vs = tensor(own[3], scales);
+        need(kc.dim() == 4 && kc.scalar_type() == at::kByte && vc.scalar_type() == at::kByte &&
+                 vc.sizes() == kc.sizes() && kc.is_contiguous() && vc.is_contiguous() && kc.size(1) <= 1024 &&
+                 kc.size(2) <= 256 && kc.size(3) <= 128,
+             codes);
+        for (const at::Tensor* s : {&ks, &vs})
+            need(s->dim() == 4 && s->scalar_type() == at::kBFloat16 && s->is_contiguous() &&
+                     s->size(0) == kc.size(0) && s->size(1) == kc.size(1) && s->size(2) == kc.size(2) &&
+                     s->size(3) == kc.size(3) / 32,
+                 scales);
+        for (const at::Tensor* t : {&ks, &vc, &vs}) need(t->device() == kc.device(), "codes and scales: on one device");
+        const bool nf4 = PyUnicode_Check(own[4]) && PyUnicode_CompareWithASCIIString(own[4], "nf4") == 0;
+        need(nf4 || (PyUnicode_Check(own[4]) && PyUnicode_CompareWithASCIIString(own[4], "fp4") == 0),
+             "quant_type: \"nf4\" or \"fp4\"");
+        c = {static_cast<uint8_t*>(kc.data_ptr()), bf16(ks), static_cast<uint8_t*>(vc.data_ptr()), bf16(vs),
+             kc.size(0), int32_t(kc.size(1)), int32_t(2 * kc.size(3)), int32_t(kc.size(2)),
+             nf4 ? NF4_QUANT_NF4 : NF4_QUANT_FP4};
+        device = kc.is_cuda() ? kc.get_device() : -1;
+    }
 };
 
-const Held* held(PyObject* o) {
-    need(PyBytes_Check(o) && PyBytes_GET_SIZE(o) == Py_ssize_t(sizeof(Held)), "cache: an NF4KVCache");
-    return reinterpret_cast<const Held*>(PyBytes_AS_STRING(o));
-}
-
-void* stream_for(const Held* cache, std::initializer_list<PyObject*> given) {
+void* stream_for(const Held& cache, std::initializer_list<PyObject*> given) {
     void* const stream = stream_for(given);
-    need(cache->device == THPVariable_Unpack(*given.begin()).get_device(), "cache: on the tensors' GPU");
+    need(cache.device == THPVariable_Unpack(*given.begin()).get_device(), "cache: on the tensors' GPU");
     return stream;
 }
 
@@ -111,33 +163,16 @@ int64_t rows(const at::Tensor& t, int64_t tokens, int64_t heads, int64_t dim, co
     return t.stride(0);
 }
 
-uint16_t* bf16(const at::Tensor& t) { return static_cast<uint16_t*>(t.data_ptr()); }
-
 const at::Tensor& rope_table(PyObject* o) {
     const at::Tensor& t = tensor(o, "table: fp32 [max_pos, rot]");
     need(t.dim() == 2 && t.scalar_type() == at::kFloat && t.is_contiguous(), "table: fp32 [max_pos, rot]");
     return t;
 }
 
-// cache(k_codes, k_scales, v_codes, v_scales, quant_type) -> bytes
+// cache(cache) -> the bytes of its nf4_kv_cache
 PyObject* cache(PyObject* const* a) {
-    const char* const codes = "codes: contiguous uint8 [pages, heads, page, dim/2]";
-    const char* const scales = "scales: contiguous bf16 [pages, heads, page, dim/64]";
-    const at::Tensor &kc = tensor(a[0], codes), &ks = tensor(a[1], scales), &vc = tensor(a[2], codes),
-                     &vs = tensor(a[3], scales);
-    need(kc.dim() == 4 && kc.scalar_type() == at::kByte && vc.scalar_type() == at::kByte && vc.sizes() == kc.sizes() &&
-             kc.is_contiguous() && vc.is_contiguous() && kc.size(1) <= 1024 && kc.size(2) <= 256 && kc.size(3) <= 128,
-         codes);
-    for (const at::Tensor* s : {&ks, &vs})
-        need(s->dim() == 4 && s->scalar_type() == at::kBFloat16 && s->is_contiguous() && s->size(0) == kc.size(0) &&
-                 s->size(1) == kc.size(1) && s->size(2) == kc.size(2) && s->size(3) == kc.size(3) / 32,
-             scales);
-    for (const at::Tensor* t : {&ks, &vc, &vs}) need(t->device() == kc.device(), "codes and scales: on one device");
-    const Held c = {{static_cast<uint8_t*>(kc.data_ptr()), bf16(ks), static_cast<uint8_t*>(vc.data_ptr()), bf16(vs),
-                     kc.size(0), int32_t(kc.size(1)), int32_t(2 * kc.size(3)), int32_t(kc.size(2)),
-                     int32(a[4], "quant_type")},
-                    kc.is_cuda() ? kc.get_device() : -1};
-    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&c), sizeof(c));
+    const Held own(a[0]);
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&own.c), sizeof(own.c));
 }
 
 // rope(x, positions, table, layout, out, backward) -> tensor
@@ -205,8 +240,8 @@ PyObject* plan(PyObject* const* a) {
 
 // append(cache, k, v, slots, positions, table, q, layout, q_out) -> q_out or None
 PyObject* append(PyObject* const* a) {
-    const Held* const own = held(a[0]);
-    const nf4_kv_cache* const c = &own->c;
+    const Held own(a[0]);
+    const nf4_kv_cache* const c = &own.c;
     const char* const kw = "k: bf16 [tokens, heads, head_dim]";
     const at::Tensor &k = tensor(a[1], kw), &v = tensor(a[2], "v: as k");
     need(k.dim() == 3, kw);
@@ -250,8 +285,8 @@ PyObject* append(PyObject* const* a) {
 
 // read(cache, slots) -> (k, v)
 PyObject* read(PyObject* const* a) {
-    const Held* const own = held(a[0]);
-    const nf4_kv_cache* const c = &own->c;
+    const Held own(a[0]);
+    const nf4_kv_cache* const c = &own.c;
     const at::Tensor& s = tensor(a[1], "slots: int64 [tokens]");
     need(s.dim() == 1, "slots: int64 [tokens]");
     const int64_t* slots = ints<int64_t>(a[1], 0, "slots: int64 [tokens]");
@@ -269,8 +304,8 @@ PyObject* read(PyObject* const* a) {
 
 // attention(cache, q, cu_q, kv_lens, block_table, max_q, max_len, scale, window, sinks, out, ws) -> out
 PyObject* attention(PyObject* const* a) {
-    const Held* const own = held(a[0]);
-    const nf4_kv_cache* const c = &own->c;
+    const Held own(a[0]);
+    const nf4_kv_cache* const c = &own.c;
     const char* const qw = "q: bf16 [total_q, q_heads, head_dim]";
     const at::Tensor& q = tensor(a[1], qw);
     need(q.dim() == 3 && q.size(1) <= INT32_MAX, qw);
@@ -359,7 +394,7 @@ PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<cache, 5>("cache"),     method<rope, 6>("rope"),
+PyMethodDef g_methods[] = {method<cache, 1>("cache"),     method<rope, 6>("rope"),
                            method<plan, 8>("plan"),       method<append, 9>("append"),
                            method<read, 2>("read"),       method<attention, 12>("attention"),
                            method<set_error, 1>("set_error"), {nullptr, nullptr, 0, nullptr}};
@@ -368,4 +403,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_nf4kv", nullptr, -1, g_methods,
 
 }  // namespace
 
-extern "C" PyMODINIT_FUNC PyInit__nf4kv() { return PyModule_Create(&g_module); }
+extern "C" PyMODINIT_FUNC PyInit__nf4kv() {
+    const char* const names[5] = {"k_codes", "k_scales", "v_codes", "v_scales", "quant_type"};
+    for (int i = 0; i < 5; ++i)
+        if (!(g_parts[i] = PyUnicode_InternFromString(names[i]))) return nullptr;
+    return PyModule_Create(&g_module);
+}

@@ -19,7 +19,7 @@ from typing import NamedTuple
 
 import torch
 
-from .nf4qlora import NF4_ELAUNCH, NF4_OK, QUANT_TYPES, NF4Error, nf4_strerror
+from .nf4qlora import NF4_ELAUNCH, NF4_OK, NF4Error, nf4_strerror
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnf4kv.so")
@@ -129,12 +129,16 @@ def nf4_rope_backward(dy, positions, table, layout: str = "half", out=None, stre
 class NF4KVCache:
     """Device buffers of a paged 4-bit cache (torch tensors): codes uint8
     [n_pages, n_heads, page_size, head_dim/2], absmax bf16 [..., head_dim/64];
-    quant_type "nf4" or "fp4"."""
+    quant_type "nf4" or "fp4".  Every call reads and checks them anew."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, quant_type: str = "nf4"):
-        self._c = _nf4kv.cache(k_codes, k_scales, v_codes, v_scales, QUANT_TYPES[quant_type])  # an nf4_kv_cache
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.quant_type = quant_type
+        _nf4kv.cache(self)  # (ValueError for parts that do not fit)
+
+    def c_struct(self) -> nf4_kv_cache:
+        """For the C functions: the addresses hold until a part is replaced."""
+        return nf4_kv_cache.from_buffer_copy(_nf4kv.cache(self))
 
     n_pages = property(lambda self: self.k_codes.shape[0])
     n_heads = property(lambda self: self.k_codes.shape[1])
@@ -186,13 +190,13 @@ def nf4_kv_append(cache: NF4KVCache, k, v, slots, positions=None, table=None, q=
     """Quantize bf16 k, v [tokens, heads, head_dim] (any token stride) into the
     cache's int64 `slots`, k rotated to `positions` by the rope `table` first
     (None: not rotated).  Returns q [tokens, q_heads, head_dim] rotated, when given."""
-    return _on(stream, _nf4kv.append, cache._c, k, v, slots, positions, table, q, ROPE_LAYOUTS[layout], q_out)
+    return _on(stream, _nf4kv.append, cache, k, v, slots, positions, table, q, ROPE_LAYOUTS[layout], q_out)
 
 
 def nf4_kv_read(cache: NF4KVCache, slots, stream=None):
     """The stored keys and values of int64 `slots`, bf16 [tokens, heads,
     head_dim] each (zeros for a slot outside the cache)."""
-    return _on(stream, _nf4kv.read, cache._c, slots)
+    return _on(stream, _nf4kv.read, cache, slots)
 
 
 def nf4_kv_attention_ws_bytes(cache: NF4KVCache, batch: int, q_heads: int, max_q: int, max_len: int, window: int = 0,
@@ -209,5 +213,5 @@ def nf4_kv_attention(cache: NF4KVCache, q, cu_q, kv_lens, block_table, max_q: in
     window > 0: only the last `window` tokens and the first `sinks` are seen.
     max_q and max_len bound every request's queries and length (max_len: by
     default what the table can hold).  scale: 1/sqrt(head_dim) by default."""
-    return _on(stream, _nf4kv.attention, cache._c, q, cu_q, kv_lens, block_table, max_q, max_len, scale, window,
+    return _on(stream, _nf4kv.attention, cache, q, cu_q, kv_lens, block_table, max_q, max_len, scale, window,
                sinks, out, ws)

@@ -1,0 +1,72 @@
+"""Host checks of how the cache library's Python layer takes its arguments (no GPU)."""
+
+import copy
+import os
+import pickle
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+pytestmark = pytest.mark.skipif(
+    not os.path.exists(os.path.join(ROOT, "bit_nf4_quantized_04_amd", "libnf4kv.so")), reason="libnf4kv.so not built")
+PARTS = ("k_codes", "k_scales", "v_codes", "v_scales")
+
+
+@pytest.fixture(scope="module")
+def K():
+    from bit_nf4_quantized_04_amd import nf4kv
+
+    return nf4kv
+
+
+def of(c):
+    """What the C functions get is what the attributes hold."""
+    s = c.c_struct()
+    assert tuple(getattr(s, n) for n in PARTS) == tuple(getattr(c, n).data_ptr() for n in PARTS)
+    assert (s.n_pages, s.n_heads, s.head_dim, s.page_size) == (c.n_pages, c.n_heads, c.head_dim, c.page_size)
+    assert s.quant_type == {"nf4": 0, "fp4": 1}[c.quant_type]
+    return {getattr(c, n).data_ptr() for n in PARTS}
+
+
+@pytest.mark.parametrize("quant", ["nf4", "fp4"])
+def test_a_cache_that_is_copied_has_its_own_buffers(K, quant):
+    c = K.nf4_kv_cache_alloc(3, 2, 128, 16, quant, device="cpu")
+    mine = of(c)
+    assert of(copy.copy(c)) == mine
+    assert not of(copy.deepcopy(c)) & mine
+    assert not of(pickle.loads(pickle.dumps(c))) & mine
+    assert of(c) == mine
+
+
+def test_a_cache_whose_buffers_are_replaced(K):
+    c = K.nf4_kv_cache_alloc(3, 2, 128, 16, device="cpu")
+    other = K.nf4_kv_cache_alloc(5, 4, 64, 32, "fp4", device="cpu")
+    before = of(c)
+    for n in PARTS:
+        setattr(c, n, getattr(c, n).clone())
+        of(c)
+    assert not of(c) & before
+    c.k_codes.resize_(3, 2, 16, 32)
+    with pytest.raises(ValueError):  # the others no longer fit
+        c.c_struct()
+    for n in (*PARTS, "quant_type"):
+        setattr(c, n, getattr(other, n))
+    assert of(c) == of(other)
+    for n, wrong in (("k_codes", other.k_scales), ("v_scales", None), ("quant_type", "int4"), ("quant_type", 0)):
+        keep = getattr(c, n)
+        setattr(c, n, wrong)
+        with pytest.raises(ValueError):
+            c.c_struct()
+        setattr(c, n, keep)
+    del c.v_codes
+    with pytest.raises(ValueError):
+        c.c_struct()
+
+
+def test_calls_want_a_cache(K):
+    import torch
+
+    slots = torch.zeros(4, dtype=torch.int64)
+    for wrong in (None, 3, b"0" * 64, slots):
+        with pytest.raises(ValueError):
+            K.nf4_kv_read(wrong, slots)
