@@ -122,7 +122,10 @@ int nf4_rope_backward(const void* dy, int64_t dy_token_stride, int64_t dy_head_s
  * its own exceed `count`, or if it asks for tokens and the tokens asked for
  * up to and with its own exceed max_tokens (requests refused for the first
  * reason want and ask nothing; those refused for the others still count, so
- * no later request overtakes them).  Then
+ * no later request overtakes them).  The step's token list holds the granted
+ * requests' tokens only, one request after the other: a caller whose rows lie
+ * by new_lens gathers them, token t of request i from row
+ * sum(new_lens[0 .. i)) + t - cu_new[i].  Then
  *   block_table   gains the granted pages, taken from the ring's head (in place)
  *   free_pages    gets the ended requests' pages at its tail, in request order (in place)
  *   free_out      {head, count} after both; not free_state itself

@@ -179,8 +179,10 @@ def nf4_kv_plan(kv_lens, new_lens, block_table, free_pages, free_state, page_siz
     """Extend int32 block_table [batch, width] (in place) by the pages that
     kv_lens + new_lens need, taken from the ring free_pages whose {head, count}
     is free_state; requests with done != 0 end and give theirs back (to the
-    ring, in place).  No host synchronization; the next step passes the
-    returned kv_lens and free_state."""
+    ring, in place).  Requests that do not fit are refused and keep their length;
+    the step's tokens are those of the others (cu_new, not new_lens, says where
+    each one's are).  No host synchronization; the next step passes the returned
+    kv_lens and free_state."""
     return NF4KVPlan(*_on(stream, _nf4kv.plan, kv_lens, new_lens, block_table, free_pages, free_state, page_size,
                           max_tokens, done))
 

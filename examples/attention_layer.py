@@ -93,10 +93,18 @@ class Server:
 
     def step(self, x, new_lens, max_new, done=None, window=0, sinks=0):
         """x [tokens, hidden]: new_lens[i] rows for each request in turn, at most
-        max_new.  A request with done != 0 ends, and takes none."""
+        max_new.  A request with done != 0 ends, and takes none; one that is refused
+        (the plan leaves its length as it was) has to come again.  The output's rows
+        are the plan's tokens: request i's are cu_new[i] to cu_new[i + 1]."""
         plan = nf4kv.nf4_kv_plan(self.lens, new_lens, self.table, self.free, self.state, self.cache.page_size,
                                  max_tokens=len(x), done=done)
         self.lens, self.state = plan.kv_lens, plan.free_state
+        # the plan's tokens are those of the granted requests, x has everybody's
+        asked = new_lens.clamp(min=0)
+        first = torch.cumsum(asked, 0) - asked
+        t = torch.arange(len(x), dtype=torch.int32, device=x.device)
+        i = torch.searchsorted(plan.cu_new[1:], t, right=True).clamp(max=self.batch - 1)
+        x = x[(first[i] + t - plan.cu_new[i]).clamp(0, max(len(x) - 1, 0))]
         return self.layer.serve(x, self.cache, plan, self.table, max_new, window, sinks, self.max_len), plan
 
 
