@@ -155,12 +155,16 @@ const T* ints(PyObject* o, int64_t n, const char* what) {
     return static_cast<const T*>(t.data_ptr());
 }
 
+// The stride of dimension d, or, since that of a single element may be any
+// number, `other` for one.
+int64_t stride(const at::Tensor& t, int d, int64_t other) { return t.size(d) == 1 ? other : t.stride(d); }
+
 // bf16 [tokens, heads, dim] with whole heads side by side: its token stride.
 int64_t rows(const at::Tensor& t, int64_t tokens, int64_t heads, int64_t dim, const char* what) {
     need(t.dim() == 3 && t.scalar_type() == at::kBFloat16 && t.size(0) == tokens && t.size(1) == heads &&
              t.size(2) == dim && t.stride(2) == 1 && (heads == 1 || t.stride(1) == dim),
          what);
-    return t.stride(0);
+    return stride(t, 0, heads * dim);
 }
 
 const at::Tensor& rope_table(PyObject* o) {
@@ -193,9 +197,11 @@ PyObject* rope(PyObject* const* a) {
         y = tensor(a[4], "out: as x");
         need(y.sizes() == x.sizes() && y.scalar_type() == x.scalar_type() && y.stride(2) == 1, "out: as x");
     }
+    const int64_t xh = stride(x, 1, x.size(2)), xt = stride(x, 0, x.size(1) * xh);
+    const int64_t yh = stride(y, 1, y.size(2)), yt = stride(y, 0, y.size(1) * yh);
     const bool back = a[5] == Py_True;
     check((back ? nf4_rope_backward : nf4_rope_forward)(
-              x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), y.stride(0), y.stride(1), x.size(0),
+              x.data_ptr(), xt, xh, y.data_ptr(), yt, yh, x.size(0),
               int32_t(x.size(1)), int32_t(x.size(2)), x.scalar_type() == at::kBFloat16, positions,
               static_cast<const float*>(t.data_ptr()), t.size(0), int32_t(t.size(1)), int32(a[3], "layout"),
               stream),
@@ -260,23 +266,21 @@ PyObject* append(PyObject* const* a) {
         positions = ints<int32_t>(a[4], tokens, "positions: int32 [tokens]");
     }
     at::Tensor q, y;
+    int64_t q_stride = 0, y_stride = 0;
     if (a[6] != Py_None) {
         const char* const qw = "q: bf16 [tokens, q_heads, head_dim], as many tokens as k, and rotated by the table";
         q = tensor(a[6], qw);
         need(table && q.dim() == 3 && q.size(1) <= INT32_MAX, qw);
-        rows(q, tokens, q.size(1), c->head_dim, qw);
+        q_stride = rows(q, tokens, q.size(1), c->head_dim, qw);
     }
     const bool has = q.defined();
     void* const stream = stream_for(own, {a[1], a[2], a[3], table ? a[4] : Py_None, a[5], a[6], a[8]});
-    if (has && a[8] == Py_None) {
-        y = made(q.sizes(), q.options());
-    } else if (has) {
-        y = tensor(a[8], "q_out: as q");
-        rows(y, tokens, q.size(1), c->head_dim, "q_out: as q");
+    if (has) {
+        y = a[8] == Py_None ? made(q.sizes(), q.options()) : tensor(a[8], "q_out: as q");
+        y_stride = rows(y, tokens, q.size(1), c->head_dim, "q_out: as q");
     }
     check(nf4_kv_append(c, bf16(k), k_stride, bf16(v), v_stride, slots, tokens, has ? bf16(q) : nullptr,
-                        has ? q.stride(0) : 0, has ? bf16(y) : nullptr, has ? y.stride(0) : 0,
-                        has ? int32_t(q.size(1)) : 0, positions, table, max_pos, int32_t(rot), int32(a[7], "layout"),
+                        q_stride, has ? bf16(y) : nullptr, y_stride, has ? int32_t(q.size(1)) : 0, positions, table, max_pos, int32_t(rot), int32(a[7], "layout"),
                         stream),
           "nf4_kv_append");
     if (has) return THPVariable_Wrap(y);
@@ -326,13 +330,8 @@ PyObject* attention(PyObject* const* a) {
         if (scale == -1.0 && PyErr_Occurred()) throw PythonError{};
     }
     void* const stream = stream_for(own, {a[1], a[2], a[3], a[4], a[10], a[11]});
-    at::Tensor y;
-    if (a[10] == Py_None) {
-        y = made(q.sizes(), q.options());
-    } else {
-        y = tensor(a[10], "out: as q");
-        rows(y, q.size(0), q.size(1), c->head_dim, "out: as q");
-    }
+    const at::Tensor y = a[10] == Py_None ? made(q.sizes(), q.options()) : tensor(a[10], "out: as q");
+    const int64_t y_stride = rows(y, q.size(0), q.size(1), c->head_dim, "out: as q");
     need(a[11] == Py_None || tensor(a[11], "ws: a contiguous tensor").is_contiguous(), "ws: a contiguous tensor");
     at::Tensor ws;
     size_t bytes = 0;
@@ -346,7 +345,7 @@ PyObject* attention(PyObject* const* a) {
     }
     check(nf4_kv_attention(c, bf16(q), q_stride, q.size(0), int32_t(q.size(1)), cu, lens,
                            static_cast<const int32_t*>(table.data_ptr()), int32_t(table.size(1)), int32_t(batch),
-                           max_q, int32_t(most), float(scale), window, sinks, bf16(y), y.stride(0),
+                           max_q, int32_t(most), float(scale), window, sinks, bf16(y), y_stride,
                            ws.defined() ? ws.data_ptr() : nullptr, bytes, stream),
           "nf4_kv_attention");
     return THPVariable_Wrap(y);

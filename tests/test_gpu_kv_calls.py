@@ -56,3 +56,54 @@ def test_a_copied_cache_is_written_and_read_by_itself(K):
         setattr(c, n, getattr(d, n))
     assert all(torch.equal(a, b) for a, b in zip(second, K.nf4_kv_read(c, slots)))
     assert torch.equal(out, K.nf4_kv_attention(c, *args, max_q=1))
+
+
+def one_token(seed, heads, dim):
+    """[1, heads, dim] as a transpose leaves it: contiguous, with another token
+    stride than a row's length."""
+    t = normal(seed, heads, 1, dim).transpose(0, 1)
+    assert t.is_contiguous() and t.stride(0) < heads * dim
+    return t
+
+
+def test_single_tokens_of_any_stride(K):
+    import torch
+
+    c, d = (K.nf4_kv_cache_alloc(3, 2, 128, 16) for _ in range(2))
+    k, v, q = one_token(1, 2, 128), one_token(2, 2, 128), one_token(3, 8, 128)
+    slots, positions, table = torch.tensor([17], device=U.dev()), i32([5]), K.nf4_rope_table(9, 128)
+    plain = [t.clone(memory_format=torch.contiguous_format).view(-1).view(t.shape) for t in (k, v, q)]
+    assert all(t.stride(0) == t[0].numel() for t in plain)
+    room = torch.zeros_like(q).view(-1)[: 8 * 128].view(8, 1, 128).transpose(0, 1)
+    want = K.nf4_kv_append(c, *plain[:2], slots, positions, table, q=plain[2])
+    assert torch.equal(want, K.nf4_kv_append(d, k, v, slots, positions, table, q=q))
+    assert torch.equal(want, K.nf4_kv_append(d, k, v, slots, positions, table, q=q, q_out=room))
+    assert all(torch.equal(a, b) for a, b in zip(K.nf4_kv_read(c, slots), K.nf4_kv_read(d, slots)))
+    args = (i32([0, 1]), i32([2]), i32([[1]]))
+    want = K.nf4_kv_attention(c, plain[2], *args, max_q=1)
+    assert torch.equal(want, K.nf4_kv_attention(d, q, *args, max_q=1))
+    room.zero_()
+    K.nf4_kv_attention(d, q, *args, max_q=1, out=room)
+    assert torch.equal(want, room)
+
+
+@pytest.mark.parametrize("fn", ["nf4_rope_forward", "nf4_rope_backward"])
+def test_rotations_of_single_tokens_and_heads(K, fn):
+    import torch
+
+    fn, table = getattr(K, fn), K.nf4_rope_table(40, 64)
+    x = one_token(4, 6, 64)
+    want = fn(x.reshape(-1).view(1, 6, 64), i32([7]), table)
+    assert torch.equal(want, fn(x, i32([7]), table))
+    room = torch.zeros(6, 1, 64, dtype=torch.bfloat16, device=U.dev()).transpose(0, 1)
+    fn(x, i32([7]), table, out=room)
+    assert torch.equal(want, room)
+    assert torch.equal(want, fn(x, i32([7]), table, out=x))
+    # one head of many tokens, its stride shorter than a head and of no whole vectors
+    y = normal(5, 33, 64)
+    odd = torch.as_strided(y, (33, 1, 64), (64, 3, 1))
+    positions = i32(np.arange(33))
+    assert torch.equal(fn(y.view(33, 1, 64), positions, table), fn(odd, positions, table))
+    room = torch.zeros_like(y)
+    fn(y.view(33, 1, 64), positions, table, out=torch.as_strided(room, (33, 1, 64), (64, 3, 1)))
+    assert torch.equal(room.view(33, 1, 64), fn(y.view(33, 1, 64), positions, table))
