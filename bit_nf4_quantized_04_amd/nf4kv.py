@@ -104,8 +104,8 @@ def nf4_rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling=None, 
 
     def make():
         t = torch.empty((max_pos, rot), dtype=torch.float32, device=device)
-        if not t.is_cuda:
-            raise ValueError("device: a GPU")
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError("device: the current GPU")
         _check(_lib.nf4_rope_table(t.data_ptr(), max_pos, rot, float(base), C.byref(s),
                                    torch.cuda.current_stream().cuda_stream), "nf4_rope_table")
         return t

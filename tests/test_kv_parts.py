@@ -70,3 +70,25 @@ def test_calls_want_a_cache(K):
     for wrong in (None, 3, b"0" * 64, slots):
         with pytest.raises(ValueError):
             K.nf4_kv_read(wrong, slots)
+
+
+def test_a_rope_table_is_made_on_the_current_gpu_only(K, monkeypatch):
+    """With tensors that say they are on GPU 1 while GPU 0 is current, and the
+    other way round, nothing is launched; with both the same it is, on the
+    tensor's address and the current stream."""
+    import types
+
+    calls = []
+    for where, current in ((1, 0), (0, 1), (1, 1)):
+        t = types.SimpleNamespace(is_cuda=True, device=types.SimpleNamespace(index=where), data_ptr=lambda: 4096)
+        cuda = types.SimpleNamespace(current_device=lambda: current,
+                                     current_stream=lambda: types.SimpleNamespace(cuda_stream=77))
+        monkeypatch.setattr(K, "torch", types.SimpleNamespace(empty=lambda *a, **k: t, float32=None, cuda=cuda))
+        monkeypatch.setattr(K, "_lib", types.SimpleNamespace(nf4_rope_table=lambda *a: calls.append(a) or 0))
+        if where != current:
+            with pytest.raises(ValueError):
+                K.nf4_rope_table(8, 64, device="cuda:%d" % where)
+            assert not calls
+        else:
+            assert K.nf4_rope_table(8, 64, device="cuda:1") is t
+            assert calls[0][:3] == (4096, 8, 64) and calls[0][-1] == 77
