@@ -1442,8 +1442,10 @@ static int launch(const Cache& c, const Attn& a, void* ws, hipStream_t st) {
     constexpr int NT2 = most_tiles(D);
     const Cut k = cut_of(D, c.n_heads, a);
     const int64_t units = int64_t(a.batch) * k.row_blocks;
-    // (a grid has below 2^32 threads, and a walk's next unit 31 bits)
-    if ((units + 8192) * c.n_heads > (k.many ? 0x7fffff : 0x7fffffff)) return NF4_EINVAL;
+    // Blocks of many rows have a workgroup of 512 threads each, of less than 2^32
+    // in a grid; few rows are walked through, where a wave's next unit, at most 8192
+    // past the last, has to fit 31 bits.
+    if (k.many ? units * c.n_heads > 0x7fffff : (units + 8192) * c.n_heads > 0x7fffffff) return NF4_EINVAL;
     Params p = {};
     for (int s = 0; s < 2; ++s) p.codes[s] = c.codes[s], p.scales[s] = c.scales[s];
     p.n_pages = uint32_t(c.n_pages);

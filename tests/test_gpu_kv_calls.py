@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 from tests import gpu_util as U
+from tests.test_gpu_kv_attention import Setup
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +108,10 @@ def test_rotations_of_single_tokens_and_heads(K, fn):
     room = torch.zeros_like(y)
     fn(y.view(33, 1, 64), positions, table, out=torch.as_strided(room, (33, 1, 64), (64, 3, 1)))
     assert torch.equal(room.view(33, 1, 64), fn(y.view(33, 1, 64), positions, table))
+
+
+def test_as_many_heads_as_a_cache_may_have(K):
+    """Single tokens and blocks of rows of 1024 heads."""
+    for lens, new in (([300, 40], [1, 1]), ([500], [100])):
+        s = Setup(K, lens, new, 1024, 1024, 64, 16, "nf4", seed=40).device()
+        s.check(s.run(), heads=(0, 511, 1023))

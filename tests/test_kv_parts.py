@@ -1,6 +1,7 @@
 """Host checks of how the cache library's Python layer takes its arguments (no GPU)."""
 
 import copy
+import ctypes as C
 import os
 import pickle
 
@@ -9,6 +10,7 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 pytestmark = pytest.mark.skipif(
     not os.path.exists(os.path.join(ROOT, "bit_nf4_quantized_04_amd", "libnf4kv.so")), reason="libnf4kv.so not built")
+EINVAL, ELAUNCH = 1, 5
 PARTS = ("k_codes", "k_scales", "v_codes", "v_scales")
 
 
@@ -92,3 +94,27 @@ def test_a_rope_table_is_made_on_the_current_gpu_only(K, monkeypatch):
         else:
             assert K.nf4_rope_table(8, 64, device="cuda:1") is t
             assert calls[0][:3] == (4096, 8, 64) and calls[0][-1] == 77
+
+
+@pytest.mark.parametrize("heads,batch,max_q", [(1024, 8191, 256), (1024, 4096, 512), (1, 65535, 32768), (8, 65535, 4096),
+                                               (1000, 40, 2048)])
+def test_blocks_of_many_rows_up_to_what_a_grid_holds(K, heads, batch, max_q):
+    """batch * n_heads * blocks of 256 rows: below 2^23 a call gets as far as the
+    launch, which fails without a GPU; from 2^23 on it is refused."""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    fake, other = C.c_void_p(0x100000), C.c_void_p(0x200000)
+    c = K.nf4_kv_cache(fake, fake, fake, fake, 10, heads, 64, 32, 0)
+
+    def call(batch, max_q, max_len=4096):
+        return K._lib.nf4_kv_attention(C.byref(c), fake, heads * 64, 1, heads, fake, fake, fake, 1 << 20, batch, max_q,
+                                       max_len, 1.0, 0, 0, other, heads * 64, None, 0, None)
+
+    blocks = lambda b, n: b * heads * -(-n // 256)  # noqa: E731
+    assert call(1, 128, 1 << 20) != EINVAL
+    b = min(batch, ((1 << 23) - 1) // blocks(1, max_q))
+    assert blocks(b, max_q) < 1 << 23 and call(b, max_q) == ELAUNCH
+    over = -(-(1 << 23) // (b * heads)) * 256
+    assert blocks(b, over) >= 1 << 23 and call(b, over) == EINVAL
