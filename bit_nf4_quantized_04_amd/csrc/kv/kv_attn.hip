@@ -384,15 +384,20 @@ struct Wave {
     __device__ __forceinline__ bool whole(int tile, const bool (&there)[2]) const {
         const int t0 = tile * kTile;
         return there[0] && there[1] && t0 + kTile - 1 <= pos_first &&
-               (p.a.window == 0 || t0 > pos_last - p.a.window || t0 + kTile <= p.a.sinks);
+               (p.a.window == 0 || t0 > before_window(pos_last) || t0 + kTile <= p.a.sinks);
     }
+
+    // The last token before the window of a row at position q; for a row that
+    // stands before the first token, and sees nothing anyway, that of the first
+    // (its own would not fit 31 bits with the largest windows).
+    __device__ __forceinline__ int before_window(int q) const { return max(q, 0) - p.a.window; }
 
     // A score that becomes -inf for the tokens that a row does not see.
     __device__ __forceinline__ void hide(int tile, const bool (&there)[2], float (&s2)[NT][2][4]) const {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const float hidden = f[t] < 0.0f ? INFINITY : -INFINITY;
-            const int after = p.a.window ? pos[t] - p.a.window : -1;  // tokens up to this one are hidden
+            const int after = p.a.window ? before_window(pos[t]) : -1;  // tokens up to this one are hidden
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -1258,7 +1263,7 @@ __global__ __launch_bounds__(64 * kWavesMany) void k_attn_many(Params p) {
         for (int j = 0; j < T / kTile; ++j) {
             const int tile = t0 + j, token = tile * kTile;
             if (idle || token > wave.pos_last) continue;
-            if (p.a.window && token + kTile - 1 <= wave.pos_first - p.a.window && token >= p.a.sinks) continue;
+            if (p.a.window && token + kTile - 1 <= wave.before_window(wave.pos_first) && token >= p.a.sinks) continue;
             auto four = [&](const float* from, int h) {
                 return *reinterpret_cast<const f32x4_t*>(from + kTile * j + 16 * h + 4 * wave.g);
             };

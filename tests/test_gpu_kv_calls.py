@@ -115,3 +115,19 @@ def test_as_many_heads_as_a_cache_may_have(K):
     for lens, new in (([300, 40], [1, 1]), ([500], [100])):
         s = Setup(K, lens, new, 1024, 1024, 64, 16, "nf4", seed=40).device()
         s.check(s.run(), heads=(0, 511, 1023))
+
+
+@pytest.mark.parametrize("lens,new,qh,kh", [([700, 90], [150, 97], 256, 256), ([50, 9000], [60, 60], 2, 1),
+                                            ([2, 9, 40] * 4, [5, 1, 3] * 4, 256, 256), ([2, 90], [6, 1], 8, 2)])
+def test_the_largest_windows(K, lens, new, qh, kh):
+    """Windows around 2^31 hide nothing, also from requests with more queries than
+    tokens, whose first ones stand before the first token: in blocks of many rows,
+    in tokens that are split, with a wave for each request and with a workgroup."""
+    import torch
+
+    s = Setup(K, lens, new, qh, kh, 64, 16, "nf4", seed=41).device()
+    want = s.run()
+    s.check(want, heads=(0, kh - 1))
+    for window in (max(lens), 2 ** 31 - 100, 2 ** 31 - 2, 2 ** 31 - 1):
+        for sinks in (0, 5, 2 ** 31 - 1):
+            assert torch.equal(want, s.run(window=window, sinks=sinks)), (window, sinks)
