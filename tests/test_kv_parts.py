@@ -43,11 +43,11 @@ def test_a_cache_that_is_copied_has_its_own_buffers(K, quant):
 def test_a_cache_whose_buffers_are_replaced(K):
     c = K.nf4_kv_cache_alloc(3, 2, 128, 16, device="cpu")
     other = K.nf4_kv_cache_alloc(5, 4, 64, 32, "fp4", device="cpu")
-    before = of(c)
+    before, keep = of(c), [getattr(c, n) for n in PARTS]  # (kept: freed addresses come back)
     for n in PARTS:
         setattr(c, n, getattr(c, n).clone())
         of(c)
-    assert not of(c) & before
+    assert not of(c) & before and len(keep) == 4
     c.k_codes.resize_(3, 2, 16, 32)
     with pytest.raises(ValueError):  # the others no longer fit
         c.c_struct()
