@@ -53,7 +53,11 @@ int rope_call(const void* x, int64_t xt, int64_t xh, void* y, int64_t yt, int64_
     const int step = is_bf16 ? 8 : 4;
     for (int64_t s : {xt, xh, yt, yh})
         if (s % step) return NF4_ESHAPE;
-    if (xh < dim || yh < dim || xt < 0 || yt < int64_t(heads - 1) * yh + dim) return NF4_EINVAL;
+    if (xh < dim || yh < dim || xt < 0) return NF4_EINVAL;
+    // the output's heads lie apart: all of a token's before the next token's, or
+    // all of a head's tokens before the next head's (quotients: no sum overflows)
+    auto within = [&](int64_t n, int64_t step, int64_t next) { return step >= dim && next >= dim && (next - dim) / step >= n - 1; };
+    if (!within(heads, yh, yt) && !within(tokens, yt, yh)) return NF4_EINVAL;
     if (x == y && (xt != yt || xh != yh)) return NF4_EINVAL;
     kv::Rope r;
     if (const int rc = rope_of(positions, table, max_pos, rot, layout, dim, false, &r)) return rc;

@@ -96,6 +96,9 @@ int nf4_rope_table(float* table, int64_t max_pos, int32_t rot, float base, const
  * in fp32 without contraction, rounded once to the type of x.  x and y:
  * `tokens` rows, token_stride apart (elements), of n_heads heads, head_stride
  * apart (>= head_dim), of head_dim consecutive elements; `is_bf16` or fp32.
+ * The heads of y do not overlap: a token's come before the next token's
+ * (y_token_stride >= (n_heads - 1) * y_head_stride + head_dim), or a head's
+ * tokens before the next head's (the same the other way round).
  * y may be x itself (same strides).  rot <= head_dim <= 512, head_dim a
  * multiple of 8.  positions: int32 [tokens]; the rotated elements of a token
  * outside [0, max_pos) are NaN.  tokens == 0 is a no-op. */

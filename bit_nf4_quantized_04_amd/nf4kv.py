@@ -115,8 +115,9 @@ def nf4_rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling=None, 
 
 def nf4_rope_forward(x, positions, table, layout: str = "half", out=None, stream=None):
     """x bf16 or fp32 [tokens, heads, head_dim] (any token and head strides: a
-    slice of a fused projection will do) with its first table.shape[1]
-    elements rotated to int32 `positions`.  out may be x."""
+    slice of a fused projection will do, or [heads, tokens, head_dim] transposed)
+    with its first table.shape[1] elements rotated to int32 `positions`.  out,
+    with strides of its own, may be x."""
     return _on(stream, _nf4kv.rope, x, positions, table, ROPE_LAYOUTS[layout], out, False)
 
 

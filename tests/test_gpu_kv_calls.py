@@ -131,3 +131,29 @@ def test_the_largest_windows(K, lens, new, qh, kh):
     for window in (max(lens), 2 ** 31 - 100, 2 ** 31 - 2, 2 ** 31 - 1):
         for sinks in (0, 5, 2 ** 31 - 1):
             assert torch.equal(want, s.run(window=window, sinks=sinks)), (window, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("tokens,heads,dim,rot,gap", [(9, 5, 64, 64, 0), (700, 40, 128, 96, 0), (33, 3, 72, 20, 8),
+                                                      (2, 2, 8, 8, 16)])
+def test_rotations_of_tensors_with_the_heads_outside(K, tokens, heads, dim, rot, gap, layout, dtype):
+    """[heads, tokens, dim] transposed, as inputs, as outputs and in place, with
+    what lies between the heads left alone."""
+    import torch
+
+    table, positions = K.nf4_rope_table(64, rot), i32(np.arange(tokens) * 7 % 64)
+    x = normal(6, tokens, heads, dim).to(getattr(torch, dtype))
+    wide = torch.full((heads, tokens * dim + gap), 3.0, dtype=x.dtype, device=U.dev())
+    outside = wide[:, : tokens * dim].unflatten(1, (tokens, dim)).transpose(0, 1)
+    assert outside.shape == x.shape and outside.stride(0) == dim
+    for fn in (K.nf4_rope_forward, K.nf4_rope_backward):
+        want = fn(x, positions, table, layout)
+        outside.zero_()
+        fn(x, positions, table, layout, out=outside)
+        assert torch.equal(want, outside)
+        outside.copy_(x)
+        assert torch.equal(want, fn(outside, positions, table, layout))
+        fn(outside, positions, table, layout, out=outside)
+        assert torch.equal(want, outside)
+    assert bool((wide[:, tokens * dim:] == 3).all())

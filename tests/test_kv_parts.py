@@ -118,3 +118,15 @@ def test_blocks_of_many_rows_up_to_what_a_grid_holds(K, heads, batch, max_q):
     assert blocks(b, max_q) < 1 << 23 and call(b, max_q) == ELAUNCH
     over = -(-(1 << 23) // (b * heads)) * 256
     assert blocks(b, over) >= 1 << 23 and call(b, over) == EINVAL
+
+
+def test_rotations_whose_outputs_would_overlap_are_refused(K):
+    fake, other = C.c_void_p(0x100000), C.c_void_p(0x200000)
+
+    def call(yt, yh, tokens=7, heads=5, dim=64):
+        return K._lib.nf4_rope_forward(fake, heads * dim, dim, other, yt, yh, tokens, heads, dim, 1, fake, fake, 9, 64, 0, None)
+
+    for yt, yh in ((64, 64), (4 * 64, 64), (64, 6 * 64), (64 + 32, 7 * 64), (0, 1 << 40), (-64, 1 << 40), (56, 1 << 20),
+                   (1 << 62, 1 << 61)):
+        assert call(yt, yh) == EINVAL, (yt, yh)
+    assert call(64, 64, tokens=1 << 40) == EINVAL
