@@ -343,7 +343,9 @@ PyObject* attention(PyObject* const* a) {
         ws = THPVariable_Unpack(a[11]);
         bytes = ws.numel() * ws.element_size();
     }
-    check(nf4_kv_attention(c, bf16(q), q_stride, q.size(0), int32_t(q.size(1)), cu, lens,
+    // (a new output has zeros where the caller's own keeps what it has)
+    const auto call = a[10] == Py_None ? nf4_kv_attention_padded : nf4_kv_attention;
+    check(call(c, bf16(q), q_stride, q.size(0), int32_t(q.size(1)), cu, lens,
                            static_cast<const int32_t*>(table.data_ptr()), int32_t(table.size(1)), int32_t(batch),
                            max_q, int32_t(most), float(scale), window, sinks, bf16(y), y_stride,
                            ws.defined() ? ws.data_ptr() : nullptr, bytes, stream),

@@ -186,6 +186,31 @@ int attn_shape(int batch, int q_heads, int n_heads, int max_q, int max_len, int 
     return NF4_OK;
 }
 
+int attn(bool zero_rest, const nf4_kv_cache* cache, const uint16_t* q, int64_t q_stride, int64_t total_q, int32_t q_heads,
+         const int32_t* cu_q, const int32_t* kv_lens, const int32_t* block_table, int32_t table_width, int32_t batch,
+         int32_t max_q, int32_t max_len, float scale, int32_t window, int32_t sinks, uint16_t* out, int64_t out_stride,
+         void* ws, size_t ws_bytes, void* stream) {
+    kv::Cache c;
+    if (const int rc = cache_of(cache, &c)) return rc;
+    if (const int rc = attn_shape(batch, q_heads, c.n_heads, max_q, max_len, window, sinks)) return rc;
+    if (total_q < 0 || total_q > 0x7fffffff || !isfinite(scale)) return NF4_EINVAL;
+    if (table_width < 0 || max_len > int64_t(table_width) << c.pshift) return NF4_EINVAL;
+    if (total_q == 0 || (max_q == 0 && !zero_rest)) return NF4_OK;
+    if (bad(q) || bad(out) || q == out) return NF4_EINVAL;
+    const int32_t* const words[] = {cu_q, kv_lens};
+    for (const int32_t* p : words)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 3)) return NF4_EINVAL;
+    if (max_len > 0 && (!block_table || (reinterpret_cast<uintptr_t>(block_table) & 3))) return NF4_EINVAL;
+    if (q_stride % 8 || out_stride % 8) return NF4_ESHAPE;
+    const int64_t row = int64_t(q_heads) * c.head_dim;
+    if (q_stride < row || out_stride < row) return NF4_EINVAL;
+    const kv::Attn a = {q, q_stride, total_q, out, out_stride, cu_q, kv_lens, block_table, table_width, batch,
+                        q_heads, max_q, max_len, window, sinks, scale};
+    const size_t need = kv::attention_ws_bytes(c, a);
+    if (need && (bad(ws) || ws_bytes < need)) return NF4_EWORKSPACE;
+    return kv::attention(c, a, zero_rest, ws, static_cast<hipStream_t>(stream));
+}
+
 }  // namespace
 
 size_t nf4_kv_attention_ws_bytes(int32_t batch, int32_t q_heads, int32_t n_heads, int32_t head_dim, int32_t max_q,
@@ -204,25 +229,17 @@ int nf4_kv_attention(const nf4_kv_cache* cache, const uint16_t* q, int64_t q_str
                      int32_t q_heads, const int32_t* cu_q, const int32_t* kv_lens, const int32_t* block_table,
                      int32_t table_width, int32_t batch, int32_t max_q, int32_t max_len, float scale, int32_t window,
                      int32_t sinks, uint16_t* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream) {
-    kv::Cache c;
-    if (const int rc = cache_of(cache, &c)) return rc;
-    if (const int rc = attn_shape(batch, q_heads, c.n_heads, max_q, max_len, window, sinks)) return rc;
-    if (total_q < 0 || total_q > 0x7fffffff || !isfinite(scale)) return NF4_EINVAL;
-    if (table_width < 0 || max_len > int64_t(table_width) << c.pshift) return NF4_EINVAL;
-    if (total_q == 0 || max_q == 0) return NF4_OK;
-    if (bad(q) || bad(out) || q == out) return NF4_EINVAL;
-    const int32_t* const words[] = {cu_q, kv_lens};
-    for (const int32_t* p : words)
-        if (!p || (reinterpret_cast<uintptr_t>(p) & 3)) return NF4_EINVAL;
-    if (max_len > 0 && (!block_table || (reinterpret_cast<uintptr_t>(block_table) & 3))) return NF4_EINVAL;
-    if (q_stride % 8 || out_stride % 8) return NF4_ESHAPE;
-    const int64_t row = int64_t(q_heads) * c.head_dim;
-    if (q_stride < row || out_stride < row) return NF4_EINVAL;
-    const kv::Attn a = {q, q_stride, total_q, out, out_stride, cu_q, kv_lens, block_table, table_width, batch,
-                        q_heads, max_q, max_len, window, sinks, scale};
-    const size_t need = kv::attention_ws_bytes(c, a);
-    if (need && (bad(ws) || ws_bytes < need)) return NF4_EWORKSPACE;
-    return kv::attention(c, a, ws, static_cast<hipStream_t>(stream));
+    return attn(false, cache, q, q_stride, total_q, q_heads, cu_q, kv_lens, block_table, table_width, batch, max_q,
+                max_len, scale, window, sinks, out, out_stride, ws, ws_bytes, stream);
+}
+
+int nf4_kv_attention_padded(const nf4_kv_cache* cache, const uint16_t* q, int64_t q_stride, int64_t total_q,
+                            int32_t q_heads, const int32_t* cu_q, const int32_t* kv_lens, const int32_t* block_table,
+                            int32_t table_width, int32_t batch, int32_t max_q, int32_t max_len, float scale,
+                            int32_t window, int32_t sinks, uint16_t* out, int64_t out_stride, void* ws,
+                            size_t ws_bytes, void* stream) {
+    return attn(true, cache, q, q_stride, total_q, q_heads, cu_q, kv_lens, block_table, table_width, batch, max_q,
+                max_len, scale, window, sinks, out, out_stride, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -101,6 +101,7 @@ struct Params {
     int step;        // few rows: a workgroup's next unit
     int splits;      // many rows: workgroups that share the tiles of a (request, block)
     float* part;     // partial results: [share][head][2][NT][part_floats(D)], or [block][split][head][8 NT][part_floats(D)]
+    int zero_rest;   // rows that are not computed get zeros
     int4* cuts;      // [share][head]: the unit that goes on in later shares: the last one, q0, rows, row0
 };
 
@@ -748,6 +749,59 @@ __device__ __forceinline__ void fill_table(char* table, const uint32_t (&levels)
     }
 }
 
+// The first request's first row of q, and the one past the last request's last.
+// Read at the start of a kernel, together with the lengths of its first unit (keep()
+// stands where those are waited for): read when zero_rest() needs them they
+// would be one more trip to memory at the end, 0.3 us of a call's 8.6.
+struct Ends {
+    int lo, hi;
+    __device__ __forceinline__ explicit Ends(const Params& p) {
+        typedef const __attribute__((address_space(4))) int32_t constant_t;
+        constant_t* cu = (constant_t*)(uintptr_t)p.a.cu_q;
+        lo = cu[0];
+        hi = cu[p.a.batch];
+    }
+    __device__ __forceinline__ void keep() const { asm volatile("" ::"s"(lo), "s"(hi)); }
+};
+
+// Zeros, where the caller wants them, in the rows of the workgroup's head that are
+// no request's, and in those past a request's max_q.  The workgroups of a head
+// share the rows out; each comes here when its own work is done, and finds
+// nothing in most calls.
+template <int D>
+__device__ __forceinline__ void zero_rest(const Params& p, const Ends& ends) {
+    if (!p.zero_rest) return;
+    const int index = p.by_heads.of(blockIdx.x), head = blockIdx.x - index * p.n_heads;
+    const int count = p.by_heads.of(gridDim.x), threads = int(blockDim.x), tid = int(threadIdx.x);
+    const int total = int(p.a.total_q), quads = p.group * (D / 8);
+    auto zero = [&](int row, int quad) {
+        *reinterpret_cast<u32x4_t*>(p.a.out + int64_t(row) * p.a.out_stride + int64_t(head) * p.group * D + 8 * quad) =
+            u32x4_t{0u, 0u, 0u, 0u};
+    };
+    const int lo = min(max(ends.lo, 0), total), hi = min(max(ends.hi, lo), total);
+    const int64_t rest = int64_t(lo + total - hi) * quads;
+    for (int64_t i = int64_t(index) * threads + tid; i < rest; i += int64_t(count) * threads) {
+        const int row = int(i / quads);
+        zero(row < lo ? row : row - lo + hi, int(i - int64_t(row) * quads));
+    }
+    if (total <= p.a.max_q) return;
+    const int l = tid & 63;
+    for (int64_t r0 = int64_t(index) * threads + tid - l; r0 < p.a.batch; r0 += int64_t(count) * threads) {
+        int from = 0, end = 0;
+        if (r0 + l < p.a.batch) {
+            from = min(max(p.a.cu_q[r0 + l], 0), total);
+            end = min(max(p.a.cu_q[r0 + l + 1], from), total);
+            from += min(end - from, p.a.max_q);
+        }
+        for (uint64_t some = __ballot(from < end); some; some &= some - 1) {
+            const int who = __builtin_ctzll(some);
+            const int a = __builtin_amdgcn_readlane(from, who), b = __builtin_amdgcn_readlane(end, who);
+            for (int row = a; row < b; ++row)
+                for (int quad = l; quad < quads; quad += 64) zero(row, quad);
+        }
+    }
+}
+
 constexpr size_t kTableBytes = 256 * 64 * 4;
 
 constexpr int kWavesMany = 8;  // of a workgroup
@@ -786,7 +840,7 @@ __host__ __device__ constexpr int groups_of_cu(int D, int nt) { return simd_wave
 // 131071 tokens 59 us (241 MB, 4.1 TB/s), one of 301 tokens 9 us; 16 requests
 // with 64 heads of 64 and a window of 1024 tokens 26.6 us (70 MB).
 template <int D, int NT, int NW>
-__global__ __launch_bounds__(64 * NW, simd_waves(D, NT)) void k_attn_few(Params p) {
+__device__ __forceinline__ void few(const Params& p, const Ends& ends) {
     using W = Wave<D, NT>;
     constexpr int kRows = 16 * NT;
     __shared__ struct {
@@ -905,6 +959,7 @@ __global__ __launch_bounds__(64 * NW, simd_waves(D, NT)) void k_attn_few(Params 
         sm.fs[side][w][l] = W::stage_row(p, q, [&](int n, int s, const u32x4_t& v) { sm.qs[side][w][n][s][l] = v; });
     };
     Part now = find();
+    ends.keep();
     if (!now.any) return;
     wave.read_ids(now.x, now.lo + w, now.hi, NW, wave.ids);
     if (w < NT) stage(now, 0);
@@ -959,6 +1014,13 @@ __global__ __launch_bounds__(64 * NW, simd_waves(D, NT)) void k_attn_few(Params 
     }
 }
 
+template <int D, int NT, int NW>
+__global__ __launch_bounds__(64 * NW, simd_waves(D, NT)) void k_attn_few(Params p) {
+    const Ends ends(p);
+    few<D, NT, NW>(p, ends);
+    zero_rest<D>(p, ends);
+}
+
 // Few rows and units for most of the GPU's waves: each wave has units of its own,
 // alone.  A workgroup has every p.step-th unit, and its waves take the next one as
 // they come free (counted in LDS), so that lengths even out; which wave has a unit
@@ -970,7 +1032,7 @@ __global__ __launch_bounds__(64 * NW, simd_waves(D, NT)) void k_attn_few(Params 
 // and workgroup: 384 requests of 400 to 500 tokens, 8 cache heads of 128 elements,
 // 48 us (188 MB, 3.9 TB/s), 99 us there; 512 with heads of 64 36 us, 64 there.
 template <int D, int NT, int NW>
-__global__ __launch_bounds__(64 * NW) void k_attn_alone(Params p) {
+__device__ __forceinline__ void alone(const Params& p, const Ends& ends) {
     using W = Wave<D, NT>;
     constexpr int kRows = 16 * NT;
     __shared__ struct {
@@ -989,6 +1051,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn_alone(Params p) {
         const int u = group + k * p.step;
         if (u >= units) return;
         const Unit x = unit_of<true>(p, u, kRows);
+        ends.keep();
         if (!x.empty) {
             const int tiles = x.tiles.count();
             wave.read_ids(x, 0, tiles, 1, wave.ids);
@@ -1009,6 +1072,13 @@ __global__ __launch_bounds__(64 * NW) void k_attn_alone(Params p) {
         if (l == 0) k = __hip_atomic_fetch_add(&sm.taken, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         k = __builtin_amdgcn_readfirstlane(k);
     }
+}
+
+template <int D, int NT, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attn_alone(Params p) {
+    const Ends ends(p);
+    alone<D, NT, NW>(p, ends);
+    zero_rest<D>(p, ends);
 }
 
 // Results of 16 rows added up over the workgroups that have them; a thread has
@@ -1141,7 +1211,7 @@ struct Frame {
 };
 
 template <int D, int NT>
-__global__ __launch_bounds__(64 * kWavesMany) void k_attn_many(Params p) {
+__device__ __forceinline__ void many(const Params& p, const Ends& ends) {
     using W = Wave<D, NT>;
     using F = Frame<D>;
     constexpr int NW = kWavesMany, T = F::T, NB = F::NB, HT = T / 16;  // HT: half tiles of a frame
@@ -1156,6 +1226,7 @@ __global__ __launch_bounds__(64 * kWavesMany) void k_attn_many(Params p) {
     const int bys = p.by_heads.of(blockIdx.x), head = blockIdx.x - bys * p.n_heads;
     const int by = p.by_splits.of(bys), split = bys - by * p.splits;
     Unit x = unit_of<true, T>(p, by, 16 * NT * NW);
+    ends.keep();
     if (x.empty) return;
     x.row0 += w * 16 * NT;
     const bool idle = x.row0 >= x.rows;  // a wave without rows, which only helps
@@ -1347,6 +1418,21 @@ __global__ __launch_bounds__(64 * kWavesMany) void k_attn_many(Params p) {
     }
 }
 
+template <int D, int NT>
+__global__ __launch_bounds__(64 * kWavesMany) void k_attn_many(Params p) {
+    const Ends ends(p);
+    many<D, NT>(p, ends);
+    zero_rest<D>(p, ends);
+}
+
+// Every row's output of a call that computes none.
+__global__ __launch_bounds__(256) void k_zero(uint16_t* out, int64_t stride, int64_t rows, int quads) {
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < rows * quads; i += gridDim.x * int64_t(256)) {
+        const int64_t row = i / quads;
+        *reinterpret_cast<u32x4_t*>(out + row * stride + 8 * (i - row * quads)) = u32x4_t{0u, 0u, 0u, 0u};
+    }
+}
+
 // How a call is cut up.
 struct Cut {
     bool many;
@@ -1443,7 +1529,7 @@ static void launch_alone(Params p, int64_t units, hipStream_t st) {
 }
 
 template <int D>
-static int launch(const Cache& c, const Attn& a, void* ws, hipStream_t st) {
+static int launch(const Cache& c, const Attn& a, bool zero_rest, void* ws, hipStream_t st) {
     constexpr int NT2 = most_tiles(D);
     const Cut k = cut_of(D, c.n_heads, a);
     const int64_t units = int64_t(a.batch) * k.row_blocks;
@@ -1457,6 +1543,7 @@ static int launch(const Cache& c, const Attn& a, void* ws, hipStream_t st) {
     p.n_heads = c.n_heads, p.pshift = c.pshift, p.qt = c.qt;
     for (int i = 0; i < 8; ++i) p.levels[i] = level_f16(c.qt, 2 * i) | level_f16(c.qt, 2 * i + 1) << 16;
     p.a = a;
+    p.zero_rest = zero_rest;
     p.group = a.q_heads / c.n_heads;
     p.row_blocks = k.row_blocks;
     p.by_group = kv::Div::by(p.group), p.by_row_blocks = kv::Div::by(p.row_blocks), p.by_heads = kv::Div::by(c.n_heads), p.by_splits = kv::Div::by(k.splits);
@@ -1491,9 +1578,16 @@ static int launch(const Cache& c, const Attn& a, void* ws, hipStream_t st) {
     return NF4_OK;
 }
 
-int attention(const Cache& c, const Attn& a, void* ws, hipStream_t st) {
-    return c.head_dim == 64 ? launch<64>(c, a, ws, st)
-         : c.head_dim == 128 ? launch<128>(c, a, ws, st) : launch<256>(c, a, ws, st);
+int attention(const Cache& c, const Attn& a, bool zero_rest, void* ws, hipStream_t st) {
+    if (a.max_q == 0) {
+        if (!zero_rest) return NF4_OK;
+        const int quads = a.q_heads * (c.head_dim / 8);
+        const int64_t blocks = std::min<int64_t>(cdiv(a.total_q * quads, 256), 4096);
+        hipLaunchKernelGGL(k_zero, dim3(unsigned(blocks)), dim3(256), 0, st, a.out, a.out_stride, a.total_q, quads);
+        return launch_status();
+    }
+    return c.head_dim == 64 ? launch<64>(c, a, zero_rest, ws, st)
+         : c.head_dim == 128 ? launch<128>(c, a, zero_rest, ws, st) : launch<256>(c, a, zero_rest, ws, st);
 }
 
 }  // namespace kv

@@ -51,7 +51,7 @@ struct Attn {
     float scale;
 };
 size_t attention_ws_bytes(const Cache& c, const Attn& a);
-int attention(const Cache& c, const Attn& a, void* ws, hipStream_t st);
+int attention(const Cache& c, const Attn& a, bool zero_rest, void* ws, hipStream_t st);
 
 
 // Division of 0 <= n < 2^31 by a number fixed on the host, as a product: with

@@ -197,13 +197,22 @@ int nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t tokens,
  * 1 <= batch <= 65535, q_heads a multiple of n_heads, q_heads / n_heads <= 128;
  * with 96 rows (queries times q_heads / n_heads) or more, batch * n_heads times
  * the rows' blocks of 256 (128 at 256 elements a head) below 2^23.
- * total_q == 0 or max_q == 0 is a no-op. */
+ * Rows of out that no request has (before cu_q[0], from cu_q[batch] on: a step
+ * whose token list has room to spare) and a request's queries past max_q are
+ * left as they are by nf4_kv_attention, and made zeros by
+ * nf4_kv_attention_padded, which is otherwise the same.
+ * total_q == 0 is a no-op, and so is max_q == 0 but for those zeros. */
 size_t nf4_kv_attention_ws_bytes(int32_t batch, int32_t q_heads, int32_t n_heads, int32_t head_dim, int32_t max_q,
                                  int32_t max_len, int32_t window, int32_t sinks);
 int nf4_kv_attention(const nf4_kv_cache* cache, const uint16_t* q, int64_t q_stride, int64_t total_q,
                      int32_t q_heads, const int32_t* cu_q, const int32_t* kv_lens, const int32_t* block_table,
                      int32_t table_width, int32_t batch, int32_t max_q, int32_t max_len, float scale, int32_t window,
                      int32_t sinks, uint16_t* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
+int nf4_kv_attention_padded(const nf4_kv_cache* cache, const uint16_t* q, int64_t q_stride, int64_t total_q,
+                            int32_t q_heads, const int32_t* cu_q, const int32_t* kv_lens, const int32_t* block_table,
+                            int32_t table_width, int32_t batch, int32_t max_q, int32_t max_len, float scale,
+                            int32_t window, int32_t sinks, uint16_t* out, int64_t out_stride, void* ws,
+                            size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

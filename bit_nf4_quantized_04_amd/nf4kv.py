@@ -47,6 +47,8 @@ class nf4_rope_scaling(C.Structure):
 
 _P, _I64, _I32 = C.c_void_p, C.c_int64, C.c_int32
 _ROPE = [_P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _I32, _P]
+_ATTENTION = [_P, _P, _I64, _I64, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, C.c_float, _I32, _I32, _P, _I64, _P,
+              C.c_size_t, _P]
 _SIGS = {
     "nf4_kv_last_hip_error": (C.c_int, []),
     "nf4_rope_table": (C.c_int, [_P, _I64, _I32, C.c_float, C.POINTER(nf4_rope_scaling), _P]),
@@ -57,8 +59,8 @@ _SIGS = {
                                 _P, _P, _I64, _I32, _I32, _P]),
     "nf4_kv_read": (C.c_int, [_P, _P, _I64, _P, _P, _P]),
     "nf4_kv_attention_ws_bytes": (C.c_size_t, [_I32] * 8),
-    "nf4_kv_attention": (C.c_int, [_P, _P, _I64, _I64, _I32, _P, _P, _P, _I32, _I32, _I32, _I32,
-                                   C.c_float, _I32, _I32, _P, _I64, _P, C.c_size_t, _P]),
+    "nf4_kv_attention": (C.c_int, _ATTENTION),
+    "nf4_kv_attention_padded": (C.c_int, _ATTENTION),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -215,6 +217,8 @@ def nf4_kv_attention(cache: NF4KVCache, q, cu_q, kv_lens, block_table, max_q: in
     kv_lens[i] cached tokens, found through int32 block_table [batch, width].
     window > 0: only the last `window` tokens and the first `sinks` are seen.
     max_q and max_len bound every request's queries and length (max_len: by
-    default what the table can hold).  scale: 1/sqrt(head_dim) by default."""
+    default what the table can hold).  scale: 1/sqrt(head_dim) by default.
+    Rows that no request has, and queries past max_q, are zeros; in a given out
+    they stay as they are."""
     return _on(stream, _nf4kv.attention, cache, q, cu_q, kv_lens, block_table, max_q, max_len, scale, window,
                sinks, out, ws)

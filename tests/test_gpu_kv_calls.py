@@ -157,3 +157,67 @@ def test_rotations_of_tensors_with_the_heads_outside(K, tokens, heads, dim, rot,
         fn(outside, positions, table, layout, out=outside)
         assert torch.equal(want, outside)
     assert bool((wide[:, tokens * dim:] == 3).all())
+
+
+def after_sevens(shape, call):
+    """The call's result in memory that held sevens before."""
+    import torch
+
+    torch.cuda.synchronize()
+    torch.full(shape, 7.0, dtype=torch.bfloat16, device=U.dev())  # freed at once: the next of its size
+    return call()
+
+
+@pytest.mark.parametrize("lens,new,qh,kh,dim", [
+    ([40, 70, 9], [1, 1, 1], 8, 2, 128), ([40, 70, 9], [6, 1, 3], 8, 2, 64), ([9000, 3000], [1, 1], 8, 2, 256),
+    ([300, 40, 90] * 30, [1, 2, 3] * 30, 128, 64, 64), ([500, 300], [150, 97], 256, 256, 64), ([2500], [256], 64, 64, 128)])
+def test_rows_that_nobody_computes(K, lens, new, qh, kh, dim):
+    """Rows in front of the first request and behind the last, and queries past
+    max_q, are zeros in an output that the call makes and stay in a given one."""
+    import torch
+
+    s = Setup(K, lens, new, qh, kh, dim, 16, "nf4", seed=42).device()
+    want = s.run()
+    n, before, behind = len(s.q), 5, 37
+    s.qd = torch.cat((s.qd[:1].expand(before, -1, -1), s.qd, s.qd[:1].expand(behind, -1, -1)))
+    s.args = (s.args[0] + before, *s.args[1:])
+    full = torch.zeros_like(s.qd)
+    full[before: before + n] = want
+    assert torch.equal(full, after_sevens(full.shape, s.run))
+    given = torch.full_like(full, 7.0)
+    s.run(out=given)
+    assert torch.equal(given[before: before + n], want)
+    assert bool((given[:before] == 7).all()) and bool((given[before + n:] == 7).all())
+    # fewer queries than a request has
+    most = max(new) - 1
+    if most:
+        got = after_sevens(full.shape, lambda: s.run(max_q=most))
+        given.fill_(7.0)
+        s.run(max_q=most, out=given)
+        for i, m in enumerate(new):
+            rows = slice(before + s.cu[i] + min(most, m), before + s.cu[i] + m)
+            assert not got[rows].any() and bool((given[rows] == 7).all()), i
+            rows = slice(before + s.cu[i], before + s.cu[i] + min(most, m))
+            assert torch.equal(got[rows], given[rows])
+        assert not got[:before].any() and not got[before + n:].any()
+    assert not after_sevens(full.shape, lambda: s.run(max_q=0)).any()
+
+
+def test_rows_that_nobody_computes_in_strided_outputs(K):
+    """The C function that makes zeros, on a slice of wider rows."""
+    import ctypes as C
+
+    import torch
+
+    s = Setup(K, [40, 70], [3, 1], 8, 2, 64, 16, "nf4", seed=43).device()
+    want, c = s.run(), s.cache.c_struct()
+    for max_q in (0, 2, 3):
+        wide = torch.full((9, 11, 64), 7.0, dtype=torch.bfloat16, device=U.dev())
+        q = torch.cat((s.qd, s.qd, s.qd[:1]))
+        assert K._lib.nf4_kv_attention_padded(
+            C.byref(c), q.data_ptr(), q.stride(0), 9, 8, *(t.data_ptr() for t in s.args), s.args[2].shape[1], 2, max_q, 70,
+            0.125, 0, 0, wide[:, 2:].data_ptr(), wide.stride(0), None, 0, torch.cuda.current_stream().cuda_stream) == 0
+        out = wide[:, 2:10]
+        assert bool((wide[:, :2] == 7).all()) and bool((wide[:, 10:] == 7).all()) and not out[4:].any()
+        assert torch.equal(out[:min(max_q, 3)], want[:min(max_q, 3)]) and not out[max_q:3].any()
+        assert torch.equal(out[3], want[3]) if max_q else not out.any()

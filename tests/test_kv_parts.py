@@ -130,3 +130,19 @@ def test_rotations_whose_outputs_would_overlap_are_refused(K):
                    (1 << 62, 1 << 61)):
         assert call(yt, yh) == EINVAL, (yt, yh)
     assert call(64, 64, tokens=1 << 40) == EINVAL
+
+
+def test_attention_with_zeros_refuses_what_attention_does(K):
+    fake, other = C.c_void_p(0x100000), C.c_void_p(0x200000)
+    c = K.nf4_kv_cache(fake, fake, fake, fake, 10, 8, 128, 32, 0)
+
+    def call(fn, q=fake, qs=4096, n=1, qh=32, w=64, b=1, mq=1, ml=2048, sc=1.0, win=0, out=other, os_=4096, ws=None, cu=fake):
+        return fn(C.byref(c), q, qs, n, qh, cu, fake, fake, w, b, mq, ml, sc, win, 0, out, os_, ws, 0, None)
+
+    for code, kw in ((0, dict(n=0, q=None)), (EINVAL, dict(n=-1)), (EINVAL, dict(b=0)), (2, dict(qh=30)), (EINVAL, dict(ml=2049)),
+                     (EINVAL, dict(win=-1)), (EINVAL, dict(q=None)), (EINVAL, dict(out=fake)), (EINVAL, dict(cu=None)),
+                     (2, dict(qs=4100)), (EINVAL, dict(os_=2048)), (EINVAL, dict(sc=float("inf"))),
+                     (4, dict(w=4096, ml=100000, b=2))):
+        assert call(K._lib.nf4_kv_attention, **kw) == call(K._lib.nf4_kv_attention_padded, **kw) == code, kw
+    assert call(K._lib.nf4_kv_attention, mq=0, out=None) == 0
+    assert call(K._lib.nf4_kv_attention_padded, mq=0, out=None) == EINVAL  # rows to fill
