@@ -86,7 +86,7 @@ int nf4_rope_table(float* table, int64_t max_pos, int32_t rot, float base, const
                    void* stream) {
     if (bad(table) || !scaling || max_pos < 1) return NF4_EINVAL;
     if (rot < 2 || rot > 512 || rot % 2) return NF4_ESHAPE;
-    if (max_pos > (int64_t(1) << 36) / rot) return NF4_EINVAL;
+    if (max_pos > (int64_t(1) << 32) / rot - 256) return NF4_EINVAL;  // a thread for each pair, 2^31 of them
     if (!isfinite(base) || base <= 1.0f || !isfinite(scaling->amplitude)) return NF4_EINVAL;
     const nf4_rope_scaling& s = *scaling;
     if (s.kind < NF4_ROPE_NONE || s.kind > NF4_ROPE_PARTS) return NF4_EUNSUPPORTED;

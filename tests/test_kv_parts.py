@@ -146,3 +146,16 @@ def test_attention_with_zeros_refuses_what_attention_does(K):
         assert call(K._lib.nf4_kv_attention, **kw) == call(K._lib.nf4_kv_attention_padded, **kw) == code, kw
     assert call(K._lib.nf4_kv_attention, mq=0, out=None) == 0
     assert call(K._lib.nf4_kv_attention_padded, mq=0, out=None) == EINVAL  # rows to fill
+
+
+def test_rope_tables_of_more_threads_than_a_grid_has(K):
+    """A thread for each pair of each position: more than 2^31 are refused, as by
+    the other calls."""
+    import torch
+
+    scaling = K.nf4_rope_scaling(0, 1.0, 1.0, 4.0, 8192.0, 1.0)
+    call = lambda max_pos, rot: K._lib.nf4_rope_table(C.c_void_p(0x100000), max_pos, rot, 10000.0, C.byref(scaling), None)  # noqa: E731
+    for max_pos, rot in ((1 << 35, 2), ((1 << 31) + 1, 2), ((1 << 25) + 1, 128), (1 << 24, 512), (1 << 62, 2)):
+        assert call(max_pos, rot) == EINVAL, (max_pos, rot)
+    if not torch.cuda.is_available():  # (the address is made up)
+        assert call((1 << 25) - 256, 128) == call((1 << 31) - 256, 2) == ELAUNCH
