@@ -31,6 +31,10 @@ int cache_of(const nf4_kv_cache* t, kv::Cache* c) {
     return c->pshift < 0 ? NF4_EUNSUPPORTED : NF4_OK;
 }
 
+// A token has more than one thread: more of them than this is more threads than a
+// grid has, and the products that a launch makes of smaller numbers fit 64 bits.
+constexpr int64_t kMostTokens = 0x7fffffff;
+
 // A rotation of rot of head_dim elements; rot == 0 (where allowed) is none.
 int rope_of(const int32_t* positions, const float* table, int64_t max_pos, int rot, int layout, int head_dim,
             bool may_be_none, kv::Rope* r) {
@@ -45,7 +49,7 @@ int rope_of(const int32_t* positions, const float* table, int64_t max_pos, int r
 int rope_call(const void* x, int64_t xt, int64_t xh, void* y, int64_t yt, int64_t yh, int64_t tokens, int heads,
               int dim, int is_bf16, const int32_t* positions, const float* table, int64_t max_pos, int rot,
               int layout, float sign, void* stream) {
-    if (tokens < 0 || heads < 1 || heads > (1 << 20) || dim < 8 || dim > 512) return NF4_EINVAL;
+    if (tokens < 0 || tokens > kMostTokens || heads < 1 || heads > (1 << 20) || dim < 8 || dim > 512) return NF4_EINVAL;
     if (dim % 8) return NF4_ESHAPE;
     if (is_bf16 != 0 && is_bf16 != 1) return NF4_EUNSUPPORTED;
     if (tokens == 0) return NF4_OK;
@@ -145,7 +149,7 @@ int nf4_kv_append(const nf4_kv_cache* cache, const uint16_t* k, int64_t k_stride
                   const float* table, int64_t max_pos, int32_t rot, int32_t layout, void* stream) {
     kv::Cache c;
     if (const int rc = cache_of(cache, &c)) return rc;
-    if (tokens < 0) return NF4_EINVAL;
+    if (tokens < 0 || tokens > kMostTokens) return NF4_EINVAL;
     if (tokens == 0) return NF4_OK;
     kv::Rope r;
     if (const int rc = rope_of(positions, table, max_pos, rot, layout, c.head_dim, true, &r)) return rc;
@@ -167,7 +171,7 @@ int nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t tokens,
                 void* stream) {
     kv::Cache c;
     if (const int rc = cache_of(cache, &c)) return rc;
-    if (tokens < 0) return NF4_EINVAL;
+    if (tokens < 0 || tokens > kMostTokens) return NF4_EINVAL;
     if (tokens == 0 || (!k_out && !v_out)) return NF4_OK;
     if (!slots || (reinterpret_cast<uintptr_t>(slots) & 7)) return NF4_EINVAL;
     if ((k_out && bad(k_out)) || (v_out && bad(v_out))) return NF4_EINVAL;

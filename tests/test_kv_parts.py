@@ -159,3 +159,14 @@ def test_rope_tables_of_more_threads_than_a_grid_has(K):
         assert call(max_pos, rot) == EINVAL, (max_pos, rot)
     if not torch.cuda.is_available():  # (the address is made up)
         assert call((1 << 25) - 256, 128) == call((1 << 31) - 256, 2) == ELAUNCH
+
+
+@pytest.mark.parametrize("tokens", [1 << 62, 1 << 60, 1 << 56, (1 << 61) + 1, 1 << 40, 1 << 31])
+def test_numbers_of_tokens_whose_products_do_not_fit(K, tokens):
+    fake, other = C.c_void_p(0x100000), C.c_void_p(0x200000)
+    c = K.nf4_kv_cache(fake, fake, fake, fake, 10, 8, 128, 32, 0)
+    for fn in (K._lib.nf4_rope_forward, K._lib.nf4_rope_backward):
+        assert fn(fake, 1024, 128, other, 1024, 128, tokens, 8, 128, 1, fake, fake, 64, 128, 0, None) == EINVAL
+    assert K._lib.nf4_kv_append(C.byref(c), fake, 1024, fake, 1024, fake, tokens, fake, 4096, other, 4096, 32, fake, fake, 64,
+                                128, 0, None) == EINVAL
+    assert K._lib.nf4_kv_read(C.byref(c), fake, tokens, fake, fake, None) == EINVAL
