@@ -1490,8 +1490,9 @@ Cut cut_of(int D, int n_heads, const kv::Attn& a) {
         // 1800 to 2048 tokens, 24 rows: 28.8 and 37.1).
         const int64_t filled = std::min(int64_t(c.row_blocks) * n_heads, at_once);
         const int64_t steps = units < at_once / n_heads ? 6 : 8;
+        // (a share's end has to fit 31 bits too: at most a tile for each share past the last)
         if (tokens * (at_once - filled) > steps * waves_few(D, c.nt) * kTile * at_once &&
-            units * (tiles + kUnitCost) < 0x7fffffff)
+            units * (tiles + kUnitCost) < 0x7fffffff - 1024)
             c.shares = int(std::max<int64_t>(at_once / n_heads, 1));
     }
     return c;

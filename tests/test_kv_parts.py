@@ -170,3 +170,12 @@ def test_numbers_of_tokens_whose_products_do_not_fit(K, tokens):
     assert K._lib.nf4_kv_append(C.byref(c), fake, 1024, fake, 1024, fake, tokens, fake, 4096, other, 4096, 32, fake, fake, 64,
                                 128, 0, None) == EINVAL
     assert K._lib.nf4_kv_read(C.byref(c), fake, tokens, fake, fake, None) == EINVAL
+
+
+def test_tiles_are_shared_while_their_sums_fit(K):
+    """Shares are laid out in sums of all units' tiles (16 more for each): a
+    workspace, which a call that shares them has, is asked for up to where a
+    share's rounded end still fits 31 bits."""
+    size = lambda tiles: K._lib.nf4_kv_attention_ws_bytes(64, 1, 1, 64, 1, 32 * tiles, 0, 0)  # noqa: E731
+    assert 64 * (33554398 + 18) == (1 << 31) - 1024 and size(33554398) == size(33554399) == 0
+    assert size(33554397) > 0
