@@ -26,8 +26,8 @@
 // exponent of the largest absmax of the token's blocks: 2^(log2 p_t - M) *
 // absmax_t is then at most 1, and the sum of the softmax keeps the same factor
 // in fp32.  M is moved only when a tile exceeds it by more than 6, and 2^8
-// more puts the weights in the upper part of fp16's range (at most 2^14, the
-// smallest kept at full precision 2^-28 of the largest).
+// more puts the weights in the upper part of fp16's range: the largest is between
+// 2^7 and 2^14, so that all down to 2^-21 of it have fp16's full precision.
 //
 // Work: a unit is a block of query rows of one request and cache head.  Rows
 // are (query, head of the group) pairs, so the heads that share a cache head

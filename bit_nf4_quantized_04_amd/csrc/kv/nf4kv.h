@@ -185,14 +185,17 @@ int nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t tokens,
  * bits down to 2^-21 of the row's largest such product and to 2^-32 of it
  * below; values of blocks whose absmax is below 2^-110 lose bits, and below
  * 2^-122 count as 0.  Scores beyond 2^26 leave fp32 no bits to
- * weigh tokens by; the result is then finite but of no meaning.
+ * weigh tokens by: the result is then of no meaning, and NaN once they, or the
+ * products of a key whose absmax is 2^115 or more, overflow fp32.
  *   q, out: bf16 [total_q][q_heads][head_dim], tokens *_stride elements apart
  *   cu_q: int32 [batch + 1]; kv_lens: int32 [batch]
  *   block_table: int32 [batch][table_width]; the tokens of a page id outside
  *     the cache are not visible
  *   max_q: at least every request's queries (later ones are not computed)
- *   max_len: at least every request's length (later tokens are not visible);
- *     at most table_width * page_size
+ *   max_len: at least every request's length; at most table_width * page_size.
+ *     A longer request is taken for one of max_len tokens: its queries stand at
+ *     the last of those.  The bounds, not the lengths, decide how a call is
+ *     cut up, so that tight ones are faster
  *   ws: nf4_kv_attention_ws_bytes() of workspace
  * 1 <= batch <= 65535, q_heads a multiple of n_heads, q_heads / n_heads <= 128;
  * with 96 rows (queries times q_heads / n_heads) or more, batch * n_heads times

@@ -217,7 +217,7 @@ def nf4_kv_attention(cache: NF4KVCache, q, cu_q, kv_lens, block_table, max_q: in
     kv_lens[i] cached tokens, found through int32 block_table [batch, width].
     window > 0: only the last `window` tokens and the first `sinks` are seen.
     max_q and max_len bound every request's queries and length (max_len: by
-    default what the table can hold).  scale: 1/sqrt(head_dim) by default.
+    default what the table can hold; a tight bound is faster).  scale: 1/sqrt(head_dim) by default.
     Rows that no request has, and queries past max_q, are zeros; in a given out
     they stay as they are."""
     return _on(stream, _nf4kv.attention, cache, q, cu_q, kv_lens, block_table, max_q, max_len, scale, window,
