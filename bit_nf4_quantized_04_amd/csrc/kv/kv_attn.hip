@@ -1465,8 +1465,8 @@ Cut cut_of(int D, int n_heads, const kv::Attn& a) {
     // Alone: units for three of five waves, and none so long that the GPU would wait
     // for it (us in k_attn_few and alone, 8 cache heads of 128: 192 requests of 16
     // to 500 tokens 38 and 31, 128 of them 27 and 32; 256 of 100 to 2000 90 and 108,
-    // 384 of them 122 and 114; 384 of 1900 to 2000 223 and 184; 384 of 300 to 3072,
-    // heads of 256, 292 and 350).
+    // 384 of them 122 and 114; 384 of 1900 to 2000 223 and 184; 384 of 300 to 3000,
+    // heads of 256, 274 and 318).
     const int64_t waves = at_once * waves_few(D, c.nt), all = units * n_heads;
     c.alone = !c.many && all * 5 >= waves * 3 && tokens <= 2048 && tokens * waves <= all * 2048;
     if (c.many) {
@@ -1479,8 +1479,8 @@ Cut cut_of(int D, int n_heads, const kv::Attn& a) {
         if (blocks <= 170) c.splits = int(std::max<int64_t>(std::min(256 / blocks, tokens / 512), 1));
     } else if (!c.alone) {
         // Six steps of every wave take about as long as a second launch (1 request,
-        // whole and shared, us: 128 elements a head, 2048 tokens 16.2 and 17.2, 3072
-        // tokens 21.3 and 17.3; 256 elements, 1536 tokens 23.7 and 23.6, 2048 tokens
+        // whole and shared, us: 128 elements a head, 2048 tokens 16.5 and 16.1, 3000
+        // tokens 21.6 and 17.0; 256 elements, 1536 tokens 23.7 and 23.6, 2048 tokens
         // 29.0 and 23.6; 64 elements, 1536 tokens 12.1 and 13.7, 2048 tokens 14.3 and
         // 14.0).  The more of the GPU one request's blocks of equal length fill, the
         // less there is to win (512 queries, 8 heads of 256, 2048 tokens: 34.4 and
